@@ -35,15 +35,15 @@ DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 def listed():
     return [
-        # one decode step's new tokens, each of another sequence, a few of them padding
-        {"name": "store_step", "op": "store", "tokens": 256, "pad": 5, "run": False, "heads": 8, "dim": 128,
-         "block": 16, "dtype": "bf16"},
+        # one decode step's new tokens, a few of them padding
+        {"name": "store_step", "op": "store", "tokens": 256, "pad": 5, "heads": 8, "dim": 128, "block": 16,
+         "dtype": "bf16"},
         # an odd count of new tokens of a small head, small blocks
-        {"name": "store_odd", "op": "store", "tokens": 777, "pad": 0, "run": True, "heads": 4, "dim": 64,
-         "block": 8, "dtype": "fp16"},
+        {"name": "store_odd", "op": "store", "tokens": 777, "pad": 0, "heads": 4, "dim": 64, "block": 8,
+         "dtype": "fp16"},
         # a prefill chunk of 64 sequences, 256 tokens each
-        {"name": "store_chunk", "op": "store", "tokens": 16384, "pad": 0, "run": True, "heads": 8, "dim": 128,
-         "block": 16, "dtype": "bf16"},
+        {"name": "store_chunk", "op": "store", "tokens": 16384, "pad": 0, "heads": 8, "dim": 128, "block": 16,
+         "dtype": "bf16"},
         # one user's short chat: latency
         {"name": "decode_one", "op": "decode", "seqs": 1, "median": 1027, "sigma": 0.0, "most": 1027, "empty": 0,
          "lens_seed": 1, "q_heads": 32, "heads": 8, "dim": 128, "block": 16, "dtype": "bf16"},
@@ -89,7 +89,6 @@ def draw(rng):
     if op == "store":
         case["tokens"] = _log(rng, 1, 16384 * 8 // max(case["heads"], 8))
         case["pad"] = rng.choice([0, 0, case["tokens"] // 7])
-        case["run"] = rng.random() < 0.5
         return case
     if op != "decode":
         case["kv"] = rng.choice(["16", "16", "fp4"])
@@ -225,11 +224,7 @@ def prepare(case, seed):
     if case["op"] == "store":
         tokens = case["tokens"]
         num_blocks = -(-tokens // block) + 3
-        if case["run"]:  # tokens of one sequence after another: whole blocks, their rows in order
-            at = torch.arange(tokens, device="cuda")
-            slots = torch.randperm(num_blocks - 1, generator=g, device="cuda")[at // block] * block + at % block
-        else:
-            slots = torch.randperm((num_blocks - 1) * block, generator=g, device="cuda")[:tokens]
+        slots = torch.randperm((num_blocks - 1) * block, generator=g, device="cuda")[:tokens]
         slots[torch.randperm(tokens, generator=g, device="cuda")[: case["pad"]]] = -1
         row = dim * 9 // 16
         return {"case": case, "slots": slots.contiguous(),
