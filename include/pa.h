@@ -492,9 +492,9 @@ typedef struct pa_token_weights {
 /*
  * pa_decode_fp4 — pa_decode over a 4-bit cache: the attention of the values
  * that the pools hold, which are exact in 16 bits: scores are summed in fp32
- * from unrounded products; for bf16 outputs each weight is rounded to 11
- * bits before it meets V, an eighth of the output's own rounding (fp16
- * outputs: to 22 bits).  Sums and statistics are fp32.
+ * from unrounded products; each weight meets V rounded to 22 bits, or to
+ * 2^-32 of the row's largest where that is more.  Sums and statistics are
+ * fp32.
  *   lse      nullable float32 device [num_seqs][num_q_heads]: as pa_decode_lse
  *   weights  nullable: accumulate the attention weights (a second launch)
  * Other arguments, results and errors as pa_decode_ex; opts may hold

@@ -16,9 +16,10 @@
 // enter mma.sync as the A operand straight from those registers.  The thin
 // products (at most 8 query rows) need a third of that path's rate.
 //
-// Rows (the kernel: pa_thin_decode.cuh).  For bf16 outputs p enters as a half:
-// its rounding, 2^-12 of each weight, is an eighth of the output's own half
-// step.  For fp16 outputs, whose half step is 2^-12, it carries its residual.
+// Rows (the kernel: pa_thin_decode.cuh).  p enters as a half and the half of its
+// rounding residual.  A half alone, off by up to 2^-11 of each weight, would do
+// for most bf16 outputs (half a step is 2^-8), but not where they nearly cancel;
+// it saves 3 % of the ragged batch below, and 7 % with 8 query heads a kv head.
 // q is rounded to half after each row is scaled by a power of two to at most
 // 2^15: exact for fp16, and for bf16 exact but for elements under 2^-29 of the
 // row's largest, whose rounding is below fp32's own.  code * scale is exact in
@@ -35,7 +36,7 @@
 // Measured (B200, one launch, D = 128): 8 sequences of 32k tokens x 40 kv heads,
 // G = 1, fp16: 274 us, 5.5 TB/s (0.84 of the copy rate; under the power cap of
 // a long loop 327); 256 sequences of log-normal lengths (median 1024) x 8, G =
-// 4, bf16: 90 us, 4.3 TB/s; one sequence of 1027 tokens x 8, G = 4: 10.  What
+// 4, bf16: 93 us, 4.2 TB/s; one sequence of 1027 tokens x 8, G = 4: 10.  What
 // is left of the roof goes to instructions: about 310 for 16 tokens and a kv
 // head, issued at 0.57 a clock, with the pipe of the conversions half busy and
 // the tensor pipe a quarter.  The warps do not wait for memory: 3 CTAs an SM
@@ -224,17 +225,15 @@ struct Fp4 {
 };
 
 template <int D, bool kScores>
-static ThinKernel pick_rows(int G, bool bf16, Variant& v) {
+static ThinKernel pick_rows(int G, Variant& v) {
   using F = Fp4<D>;
-  if (G == 8) return bf16 ? thin_kernel<F, true, kScores, false>(G, v) : thin_kernel<F, true, kScores, true>(G, v);
-  return bf16 ? thin_kernel<F, false, kScores, false>(G, v) : thin_kernel<F, false, kScores, true>(G, v);
+  return G == 8 ? thin_kernel<F, true, kScores>(G, v) : thin_kernel<F, false, kScores>(G, v);
 }
 
 static ThinKernel select_fp4(const pa_pool_desc& pool, int G, bool scores, Variant& v) {
   if (G != 1 && G != 2 && G != 4 && G != 8) return nullptr;
-  const bool bf16 = pool.dtype == PA_BF16;
-  if (pool.head_dim == 128) return scores ? pick_rows<128, true>(G, bf16, v) : pick_rows<128, false>(G, bf16, v);
-  return scores ? pick_rows<64, true>(G, bf16, v) : pick_rows<64, false>(G, bf16, v);
+  if (pool.head_dim == 128) return scores ? pick_rows<128, true>(G, v) : pick_rows<128, false>(G, v);
+  return scores ? pick_rows<64, true>(G, v) : pick_rows<64, false>(G, v);
 }
 
 static bool opts_fine(const pa_decode_opts* opts) {

@@ -12,8 +12,7 @@
 //   S^T[token, row] = K[token, d] q^T[d, row]      16 x 8, D/16 steps
 //   O^T[d, row]    += V^T[d, token] p^T[token, row]  D/16 tiles of 16 x 8
 //
-// Rows.  The 8 columns are the G query heads of the kv head.  With kResidual p
-// enters as a 16-bit value and the 16-bit value of its rounding residual (22
+// Rows.  The 8 columns are the G query heads of the kv head.  p enters as a 16-bit value and the 16-bit value of its rounding residual (22
 // significant bits in halves, of a p within 2^-8 of the largest, and 2^-32 of
 // that below; 16 in bf16): for G <= 4 columns 4..7 repeat the query rows, so
 // their threads compute the same p and pass on the residual, and the two halves
@@ -363,7 +362,7 @@ struct State {
 // One step of 32 tokens: scores, softmax, O^T.  `left`: valid tokens from its
 // first one on.  In c, d and p: index 0, 1 the columns 2t, 2t + 1 of token g,
 // 2, 3 those of token g + 8, of each half.
-template <class F, bool kEight, bool kScores, bool kResidual>
+template <class F, bool kEight, bool kScores>
 __device__ __forceinline__ void step(const ThinParams& p, const uint8_t* slot, int lane, int left,
                                      const Unit<F::kD, kEight ? 8 : 4>& unit, float f0, float f1, State<F::kD>& st,
                                      float* scores) {
@@ -450,18 +449,16 @@ __device__ __forceinline__ void step(const ThinParams& p, const uint8_t* slot, i
       st.l0 += p0;
       st.l1 += p1;
       uint32_t w = pack2<F::kBf16P>(p0, p1);
-      if constexpr (kResidual) {
-        float h0, h1;
-        unpack2<F::kBf16P>(w, h0, h1);
-        if constexpr (kEight) {
-          d[i] = transpose8x8(pack2<F::kBf16P>(p0 - h0, p1 - h1));
-        } else {
-          w = pack2<F::kBf16P>(fmaf(-keep, h0, p0), fmaf(-keep, h1, p1));
-        }
+      float h0, h1;
+      unpack2<F::kBf16P>(w, h0, h1);
+      if constexpr (kEight) {
+        d[i] = transpose8x8(pack2<F::kBf16P>(p0 - h0, p1 - h1));
+      } else {
+        w = pack2<F::kBf16P>(fmaf(-keep, h0, p0), fmaf(-keep, h1, p1));
       }
       b[i] = transpose8x8(w);
     }
-    F::template values<kEight && kResidual>(slot, 16 * k, lane, b[0], b[1], d[0], d[1], st.acc);
+    F::template values<kEight>(slot, 16 * k, lane, b[0], b[1], d[0], d[1], st.acc);
   }
 }
 
@@ -692,7 +689,7 @@ __device__ __forceinline__ void empty_rows(const ThinParams& p) {
   }
 }
 
-template <class F, bool kEight, bool kScores, bool kResidual>
+template <class F, bool kEight, bool kScores>
 __global__ void __launch_bounds__(kDecodeThreads, F::kCtasPerSm) decode_thin_kernel(const ThinParams p) {
   constexpr int kRows = kEight ? 8 : 4;
   constexpr int D = F::kD;
@@ -747,7 +744,7 @@ __global__ void __launch_bounds__(kDecodeThreads, F::kCtasPerSm) decode_thin_ker
       ld.issue(p, sm.ahead[warp], ring_at + (slot ^ 1) * F::kBytes, warp, lane);
       cp_wait<1>();
       __syncwarp();
-      step<F, kEight, kScores, kResidual>(p, ring + slot * F::kBytes, lane, len - (tok0 + i * kStepTok), unit,
+      step<F, kEight, kScores>(p, ring + slot * F::kBytes, lane, len - (tok0 + i * kStepTok), unit,
                                           f.x, f.y, st,
                                           kScores ? scores + static_cast<size_t>(i) * kStepTok * G : nullptr);
       slot ^= 1;
@@ -763,7 +760,7 @@ __global__ void __launch_bounds__(kDecodeThreads, F::kCtasPerSm) decode_thin_ker
       st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
       st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
     }
-    if constexpr (!kEight && kResidual) {  // the residuals' half of O
+    if constexpr (!kEight) {  // the residuals' half of O
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
@@ -835,9 +832,9 @@ __global__ void __launch_bounds__(kDecodeThreads, F::kCtasPerSm) decode_thin_ker
 
 // The instance's launch values, and its kernel.
 using ThinKernel = void (*)(const ThinParams);
-template <class F, bool kEight, bool kScores, bool kResidual>
+template <class F, bool kEight, bool kScores>
 ThinKernel thin_kernel(int G, Variant& v) {
-  ThinKernel kernel = &decode_thin_kernel<F, kEight, kScores, kResidual>;
+  ThinKernel kernel = &decode_thin_kernel<F, kEight, kScores>;
   v.kernel = reinterpret_cast<const void*>(kernel);
   v.threads = kDecodeThreads;
   v.smem_bytes = static_cast<int>(sizeof(ThinSmem<F, kEight ? 8 : 4>));

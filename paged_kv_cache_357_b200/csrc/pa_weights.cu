@@ -18,7 +18,7 @@
 // Measured (B200): decode and weights of 256 sequences (log-normal lengths,
 // median 1024, 8 kv heads, G = 4, D = 128, 16-bit pools) 234 us, 5.9 TB/s of
 // what the two must move (0.91 of the copy rate); 245 with scores that go to
-// memory and come back.  128 sequences of 2304 tokens, G = 8, 4-bit pools: 104
+// memory and come back.  128 sequences of 2304 tokens, G = 8, 4-bit pools: 111
 // us, of which this launch is about 12.
 #include <cuda_runtime.h>
 

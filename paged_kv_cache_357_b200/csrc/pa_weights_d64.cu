@@ -138,13 +138,13 @@ static cudaError_t launch_wide(const Variant& v, const DecodeParams& prm, int ct
   p.G = prm.num_q_heads / prm.num_kv_heads;
   p.bf16 = kBf16;
   p.out_scale = 1.f;
-  return launch_overlapped(&decode_thin_kernel<Wide<kBf16>, kEight, true, true>, dim3(ctas), dim3(kDecodeThreads),
+  return launch_overlapped(&decode_thin_kernel<Wide<kBf16>, kEight, true>, dim3(ctas), dim3(kDecodeThreads),
                            static_cast<size_t>(v.smem_bytes), stream, p);
 }
 
 template <bool kBf16, bool kEight>
 static void pick_wide(int block_size, int G, Variant& v) {
-  thin_kernel<Wide<kBf16>, kEight, true, true>(G, v);
+  thin_kernel<Wide<kBf16>, kEight, true>(G, v);
   v.launch = block_size == 8    ? &launch_wide<kBf16, kEight, 8>
              : block_size == 16 ? &launch_wide<kBf16, kEight, 16>
                                 : &launch_wide<kBf16, kEight, 32>;
