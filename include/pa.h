@@ -521,7 +521,10 @@ PA_API pa_status pa_decode_fp4(const void* q, const void* k_pool, const void* v_
 
 /*
  * pa_decode_weights — pa_decode over 16-bit pools that also accumulates the
- * attention weights (see pa_token_weights; a second launch).  head_dim 64 and
+ * attention weights (see pa_token_weights; a second launch).  The output is
+ * pa_decode's bit for bit at head_dim 128; at 64 another kernel answers, whose
+ * sums run in another order and whose weights meet V rounded to 22 (fp16) or
+ * 24 bits (bf16).  head_dim 64 and
  * 128, group sizes 1, 2, 4 and 8, blocks of 8, 16 or 32, max_blocks_per_seq *
  * block_size up to 2^30; opts may hold num_ctas only (flags:
  * PA_ERR_UNSUPPORTED).  Other arguments, results and errors as

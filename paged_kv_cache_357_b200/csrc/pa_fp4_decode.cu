@@ -174,11 +174,11 @@ struct Fp4 {
 
   // O^T += V^T p^T of 16 tokens, rows `at` of the slot.  This thread's tokens
   // are 2t, 2t + 1, 2t + 8, 2t + 9, its d's D/8 neighbours; tile i's rows g and
-  // g + 8 are their pair 2i, 2i + 1.  (b0, b1): p; (d0, d1): its residual, where
-  // that is a second product.
-  template <bool kSecond>
-  __device__ static __forceinline__ void values(const uint8_t* slot, int at, int lane, uint32_t b0, uint32_t b1,
-                                                uint32_t d0, uint32_t d1, float (&acc)[D / 16][4]) {
+  // g + 8 are their pair 2i, 2i + 1.  b: p, and its residual where that is a
+  // second product.
+  template <int kParts>
+  __device__ static __forceinline__ void values(const uint8_t* slot, int at, int lane, const uint32_t (&b)[kParts][2],
+                                                float (&acc)[D / 16][4]) {
     const int g = lane >> 2, t = lane & 3;
     constexpr int kVW = D / 64;  // words of codes a thread reads of each row
     uint32_t v[4][kVW], sv[2];
@@ -208,8 +208,8 @@ struct Fp4 {
       for (int j = 0; j < 4; ++j) {
         const uint32_t a0 = hmul2(lo[j], sv[0]), a1 = hmul2(hi[j], sv[0]);
         const uint32_t a2 = hmul2(lo8[j], sv[1]), a3 = hmul2(hi8[j], sv[1]);
-        mma_f16(acc[4 * w + j], a0, a1, a2, a3, b0, b1);
-        if constexpr (kSecond) mma_f16(acc[4 * w + j], a0, a1, a2, a3, d0, d1);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) mma_f16(acc[4 * w + j], a0, a1, a2, a3, b[i][0], b[i][1]);
       }
     }
   }

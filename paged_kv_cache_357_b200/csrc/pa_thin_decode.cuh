@@ -12,11 +12,13 @@
 //   S^T[token, row] = K[token, d] q^T[d, row]      16 x 8, D/16 steps
 //   O^T[d, row]    += V^T[d, token] p^T[token, row]  D/16 tiles of 16 x 8
 //
-// Rows.  The 8 columns are the G query heads of the kv head.  p enters as a 16-bit value and the 16-bit value of its rounding residual (22
-// significant bits in halves, of a p within 2^-8 of the largest, and 2^-32 of
-// that below; 16 in bf16): for G <= 4 columns 4..7 repeat the query rows, so
-// their threads compute the same p and pass on the residual, and the two halves
-// of O are added at the end; for G = 8 the residual is a second product.
+// Rows.  The 8 columns are the G query heads of the kv head.  p enters as a
+// 16-bit value and the 16-bit value of its rounding residual: 22 significant
+// bits in halves, of a p within 2^-8 of the largest, and 2^-32 of that below.
+// In bf16 these are 16 bits (2^-17 of p), so a third value takes what is left:
+// 24.  For G <= 4 columns 4..7 repeat the query rows, so their threads compute
+// the same p and pass on the residual, and the two halves of O are added at the
+// end; for G = 8 the residual is a second product.  The third value is one more.
 //
 // Work.  Ranges of equal cost per CTA (pa_decode_common.cuh) in granules of
 // 128 tokens; the 4 warps of a CTA take 32-token steps in turn, each with
@@ -438,27 +440,36 @@ __device__ __forceinline__ void step(const ThinParams& p, const uint8_t* slot, i
       }
     }
   }
-  // p as halves; columns 4..7 (kEight: a second product) take the residuals
+  // p as 16-bit values; columns 4..7 (kEight: a second product) take the
+  // residuals, and one more product what bf16 leaves of those
   const float keep = t < 2 ? 0.f : 1.f;
+  constexpr int kParts = (kEight ? 2 : 1) + (F::kBf16P ? 1 : 0);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    uint32_t b[2], d[2] = {0u, 0u};
+    uint32_t b[kParts][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float p0 = fast_exp2(x[k][2 * i]), p1 = fast_exp2(x[k][2 * i + 1]);
       st.l0 += p0;
       st.l1 += p1;
-      uint32_t w = pack2<F::kBf16P>(p0, p1);
+      const uint32_t head = pack2<F::kBf16P>(p0, p1);
       float h0, h1;
-      unpack2<F::kBf16P>(w, h0, h1);
-      if constexpr (kEight) {
-        d[i] = transpose8x8(pack2<F::kBf16P>(p0 - h0, p1 - h1));
+      unpack2<F::kBf16P>(head, h0, h1);
+      if constexpr (kEight || F::kBf16P) {
+        const uint32_t rest = pack2<F::kBf16P>(p0 - h0, p1 - h1);
+        b[0][i] = transpose8x8(kEight || t < 2 ? head : rest);
+        if constexpr (kEight) b[1][i] = transpose8x8(rest);
+        if constexpr (F::kBf16P) {
+          float r0, r1;
+          unpack2<true>(rest, r0, r1);
+          const uint32_t last = pack2<true>(p0 - h0 - r0, p1 - h1 - r1);
+          b[kParts - 1][i] = transpose8x8(kEight || t < 2 ? last : 0u);
+        }
       } else {
-        w = pack2<F::kBf16P>(fmaf(-keep, h0, p0), fmaf(-keep, h1, p1));
+        b[0][i] = transpose8x8(pack2<F::kBf16P>(fmaf(-keep, h0, p0), fmaf(-keep, h1, p1)));
       }
-      b[i] = transpose8x8(w);
     }
-    F::template values<kEight>(slot, 16 * k, lane, b[0], b[1], d[0], d[1], st.acc);
+    F::template values<kParts>(slot, 16 * k, lane, b, st.acc);
   }
 }
 

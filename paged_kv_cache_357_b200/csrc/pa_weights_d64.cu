@@ -6,8 +6,8 @@
 // head) pair is 256 bytes, and G products of each of its 128 elements: on CUDA
 // cores the instructions outlast the copies, and the tensor-core kernel's tiles
 // are of head_dim 128.  q and the pools enter as they are; p as a 16-bit value and its
-// residual, 16 bits in bf16 (2^-17 of each weight, 1/256 of the output's own
-// rounding) and 22 in fp16.
+// residual (22 bits) in fp16, and in bf16, where those two hold 16 bits, as
+// three values (24): pa_decode takes p in fp32 at this head_dim.
 //
 // Rows are 128 bytes, a line each: their 16-byte pieces are placed by the
 // exclusive-or with the row's number, so that ldmatrix reads 8 rows without a
@@ -91,11 +91,10 @@ struct Wide {
   }
 
   // O^T += V^T p^T of 16 tokens, rows `at` of the slot: tile i is d's 16 i to
-  // 16 i + 15.  (b0, b1): p; (d0, d1): its residual, where that is a second
-  // product.
-  template <bool kSecond>
-  __device__ static __forceinline__ void values(const uint8_t* slot, int at, int lane, uint32_t b0, uint32_t b1,
-                                                uint32_t d0, uint32_t d1, float (&acc)[kD / 16][4]) {
+  // 16 i + 15.  b: p's values, a product each.
+  template <int kParts>
+  __device__ static __forceinline__ void values(const uint8_t* slot, int at, int lane, const uint32_t (&b)[kParts][2],
+                                                float (&acc)[kD / 16][4]) {
     const uint32_t v = smem_u32(slot) + kV;
     const int tok = at + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
@@ -105,8 +104,8 @@ struct Wide {
                    : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
                    : "r"(piece_at(v, tok, 2 * i + ((lane >> 3) & 1)))
                    : "memory");
-      mma(acc[i], a, b0, b1);
-      if constexpr (kSecond) mma(acc[i], a, d0, d1);
+#pragma unroll
+      for (int j = 0; j < kParts; ++j) mma(acc[i], a, b[j][0], b[j][1]);
     }
   }
 

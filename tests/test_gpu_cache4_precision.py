@@ -70,3 +70,19 @@ def test_weights_over_4_bit_pools_keep_their_bits(cuda_device, dtype, G, D, weig
     pa.pa_decode_fp4(q.to(cuda_device), kp, vp, dev(tables, cuda_device), dev(np.array(LENS, np.int32), cuda_device), 1.0,
                      got, pa.alloc_decode_fp4_workspace(S, 2 * G, kp, width if weighted else 0), weights=w)
     assert_close(got, out, A, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_weights_over_16_bit_pools_at_head_dim_64_keep_their_bits(cuda_device, dtype, G):
+    import torch
+
+    import paged_kv_cache_357_b200 as pa
+
+    q, k, v, tables, out, A = pairs([G, 64], G, 64, dtype)
+    kp, vp = (torch.from_numpy(x).to(ref.torch_type(dtype)).to(cuda_device) for x in (k, v))
+    S = len(LENS)
+    got, w = torch.full_like(q, float("nan")).to(cuda_device), torch.zeros((S, 2, 8), device=cuda_device)
+    pa.pa_decode_weights(q.to(cuda_device), kp, vp, dev(tables, cuda_device), dev(np.array(LENS, np.int32), cuda_device),
+                         1.0, w, got, pa.alloc_decode_weights_workspace(S, 2 * G, kp, 1))
+    assert_close(got, out, A, dtype)
