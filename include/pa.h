@@ -478,8 +478,11 @@ PA_API pa_status pa_copy_blocks_fp4(const int64_t* src_dst_pairs, int32_t num_pa
  * first decode after a prefill).  Entries past the sequence's length are
  * left as they are.  fp32, one addition an entry in a fixed order: the same
  * inputs give the same bits.
- * Two sequences of a call with the same row: undefined.  PA_DEV_BAD_ROW: a
- * row outside [0, num_rows), that sequence's entries are left as they are.
+ * Two sequences of a call with the same row: undefined.  A sequence's entries
+ * are left as they are on PA_DEV_BAD_ROW (a row outside [0, num_rows)),
+ * PA_DEV_BAD_SEQ_LEN and PA_DEV_BAD_BLOCK_ID; on PA_DEV_TIMEOUT those of every
+ * sequence, in this call and (with the same status) in later ones until the
+ * workspace is zeroed again.
  */
 typedef struct pa_token_weights {
   float* weights;       /* device [num_rows][num_kv_heads][row_tokens], 4-byte aligned */
@@ -524,9 +527,9 @@ PA_API pa_status pa_decode_fp4(const void* q, const void* k_pool, const void* v_
  * attention weights (see pa_token_weights; a second launch).  The output is
  * pa_decode's bit for bit at head_dim 128; at 64 another kernel answers, whose
  * sums run in another order and whose weights meet V rounded to 22 (fp16) or
- * 24 bits (bf16).  head_dim 64 and
- * 128, group sizes 1, 2, 4 and 8, blocks of 8, 16 or 32, max_blocks_per_seq *
- * block_size up to 2^30; opts may hold num_ctas only (flags:
+ * 24 bits (bf16).  head_dim 64 and 128, group sizes 1, 2, 4 and 8, blocks of
+ * 8, 16 or 32, max_blocks_per_seq * block_size up to 2^30; opts may hold
+ * num_ctas and, at head_dim 128, PA_DECODE_TEST_WITHHOLD_COPIES (other flags:
  * PA_ERR_UNSUPPORTED).  Other arguments, results and errors as
  * pa_decode_ex.  The workspace also holds the scores between the launches; it
  * serves calls of any num_seqs and max_blocks_per_seq that it is large enough

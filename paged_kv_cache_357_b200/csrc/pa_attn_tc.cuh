@@ -132,6 +132,14 @@ __host__ __device__ constexpr bool is_multi(int mode) { return mode == kMulti ||
 // own, so that the plain decode's softmax carries no store).
 __host__ __device__ constexpr bool is_decode(int mode) { return mode == kDecode || mode == kDecodeScores; }
 
+// A wait ran out.  kDecodeScores: the scores or normalisers are not all there,
+// which the launch that adds weights up has to know.
+template <int kMode>
+__device__ __forceinline__ void record_timeout(const DecodeParams& p) {
+  record_status(p.status, PA_DEV_TIMEOUT);
+  if constexpr (kMode == kDecodeScores) atomicExch(p.grid_sync + kScoresFailed, 1);
+}
+
 // Shapes that follow from the number of query rows R of a unit.  P enters
 // the PV product as two 16-bit rows per query row, p = hi + lo (the head and
 // the rounding residual), so PV keeps about 16 significant bits of each
@@ -1090,7 +1098,7 @@ __global__ void __launch_bounds__(Rows<G * RG>::kThreads, 1)
       }
       if (!ok) {
         sm.abort = 1;
-        record_status(p.status, PA_DEV_TIMEOUT);
+        record_timeout<kMode>(p);
       }
     }
   } else if (warp == kQKWarp) {
@@ -1135,7 +1143,7 @@ __global__ void __launch_bounds__(Rows<G * RG>::kThreads, 1)
       sm.q_consumed = seg_i;
       if (!ok) {
         sm.abort = 1;
-        record_status(p.status, PA_DEV_TIMEOUT);
+        record_timeout<kMode>(p);
       }
     }
     __syncwarp();
@@ -1185,7 +1193,7 @@ __global__ void __launch_bounds__(Rows<G * RG>::kThreads, 1)
       sm.v_consumed = pv;
       if (!ok) {
         sm.abort = 1;
-        record_status(p.status, PA_DEV_TIMEOUT);
+        record_timeout<kMode>(p);
       }
     }
     __syncwarp();
@@ -1567,7 +1575,7 @@ __global__ void __launch_bounds__(Rows<G * RG>::kThreads, 1)
         if (got) {
           atomicSub(reinterpret_cast<unsigned int*>(counter), need << shift);  // back to zero for the next launch
         } else {
-          record_status(p.status, PA_DEV_TIMEOUT);
+          record_timeout<kMode>(p);
         }
         sm.merge_ok[wg] = got;
       }
@@ -1642,7 +1650,7 @@ __global__ void __launch_bounds__(Rows<G * RG>::kThreads, 1)
     }
     if (!ok && lane == 0) {
       sm.abort = 1;
-      record_status(p.status, PA_DEV_TIMEOUT);
+      record_timeout<kMode>(p);
     }
   }
 

@@ -785,11 +785,12 @@ static size_t counters_room(size_t both) { return align_up(both / 33, 256); }
 static size_t with_counters(size_t scores) { return scores + scores / 32 + 512; }
 
 // The kernel of pa_decode_weights: the tensor-core decode with scores at
-// head_dim 128, the thin decode at 64.  Neither takes flags.
+// head_dim 128, the thin decode at 64.  The first has waits that the test hook
+// can make run out; no other flag is taken.
 static bool select_scores_variant(const pa_pool_desc& pool, int num_q_heads, int flags, Variant& v) {
   int G = 0;
-  if (flags != 0 || !group_of(pool, num_q_heads, G)) return false;
-  return select_tc_scores(pool, G, v) || select_scores_d64(pool, G, v);
+  if ((flags & ~PA_DECODE_TEST_WITHHOLD_COPIES) != 0 || !group_of(pool, num_q_heads, G)) return false;
+  return select_tc_scores(pool, G, v) || (flags == 0 && select_scores_d64(pool, G, v));
 }
 
 extern "C" size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
@@ -833,8 +834,8 @@ extern "C" pa_status pa_decode_weights(const void* q, const void* k_pool, const 
   split_scores(static_cast<char*>(workspace) + base, num_seqs, num_q_heads, &prm.lse, &prm.scores);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (v.launch(v, prm, ctas, s) != cudaSuccess) return PA_ERR_CUDA;
-  return accumulate_weights(prm.scores, prm.lse, *weights, seq_lens, num_seqs, num_q_heads, max_blocks_per_seq,
-                            dev_status, pool, s);
+  return accumulate_weights(prm.scores, prm.lse, *weights, block_tables, seq_lens, num_seqs, num_q_heads,
+                            max_blocks_per_seq, prm.grid_sync + kScoresFailed, dev_status, pool, s);
 }
 
 extern "C" pa_status pa_decode_ex(const void* q, const void* k_pool, const void* v_pool,

@@ -87,8 +87,10 @@ __device__ __forceinline__ float* score_row(const DecodeParams& p, int s, int h,
 }
 
 // Workspace bytes of the grid-wide barrier's words (one 128-byte line used),
-// between the partial states and the arrival counters.
+// between the partial states and the arrival counters; the word in the next
+// line is 1 after a decode for pa_decode_weights whose waits ran out.
 constexpr int kGridSyncBytes = 256;
+constexpr int kScoresFailed = 32;
 
 constexpr long long kGranuleCost = 8;  // partition cost of one granule
 

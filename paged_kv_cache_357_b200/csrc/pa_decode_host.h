@@ -77,10 +77,13 @@ long long score_tokens_of(int max_blocks_per_seq, int block_size);
 size_t scores_bytes(int num_seqs, int num_q_heads, int max_blocks_per_seq, int block_size);
 void split_scores(char* base, int num_seqs, int num_q_heads, float** norm2, float** scores);
 bool token_weights_ok(const pa_token_weights* w, int max_blocks_per_seq, int num_seqs, const pa_pool_desc* pool);
-// Adds 2^(score - normaliser) over each kv head's query heads to the rows.
+// Adds 2^(score - normaliser) over each kv head's query heads to the rows; to
+// none of them if *failed (or null), and not to those of a sequence with a bad
+// entry in its table.
 pa_status accumulate_weights(const float* scores, const float* norm2, const pa_token_weights& w,
-                             const int32_t* seq_lens, int num_seqs, int num_q_heads, int max_blocks_per_seq,
-                             int32_t* dev_status, const pa_pool_desc* pool, cudaStream_t stream);
+                             const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                             int max_blocks_per_seq, const int32_t* failed, int32_t* dev_status,
+                             const pa_pool_desc* pool, cudaStream_t stream);
 
 // Tensor-core decode instances that also write scores and normalisers
 // (pa_decode_tc_scores.cu and its instance files), if one exists.

@@ -315,6 +315,6 @@ extern "C" pa_status pa_decode_fp4(const void* q, const void* k_pool, const void
       cudaSuccess)
     return PA_ERR_CUDA;
   if (weights == nullptr) return PA_OK;
-  return accumulate_weights(p.scores, p.norm2, *weights, seq_lens, num_seqs, num_q_heads, max_blocks_per_seq,
-                            dev_status, pool, s);
+  return accumulate_weights(p.scores, p.norm2, *weights, block_tables, seq_lens, num_seqs, num_q_heads,
+                            max_blocks_per_seq, nullptr, dev_status, pool, s);
 }

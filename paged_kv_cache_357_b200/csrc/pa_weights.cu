@@ -16,9 +16,9 @@
 // order of memory.
 //
 // Measured (B200): decode and weights of 256 sequences (log-normal lengths,
-// median 1024, 8 kv heads, G = 4, D = 128, 16-bit pools) 234 us, 5.9 TB/s of
+// median 1024, 8 kv heads, G = 4, D = 128, 16-bit pools) 237 us, 5.9 TB/s of
 // what the two must move (0.91 of the copy rate); 245 with scores that go to
-// memory and come back.  128 sequences of 2304 tokens, G = 8, 4-bit pools: 111
+// memory and come back.  128 sequences of 2304 tokens, G = 8, 4-bit pools: 113
 // us, of which this launch is about 12.
 #include <cuda_runtime.h>
 
@@ -38,24 +38,38 @@ struct WeightParams {
   float* weights;
   const int32_t* rows;
   const int32_t* seq_lens;
+  const int32_t* tables;
+  const int32_t* failed;  // of the decode, or null
   int32_t* status;
   long long score_tokens, row_tokens;
   int num_rows, num_new, num_heads, num_q_heads, max_tokens;
+  int table_width, block_size, num_blocks;
 };
 
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads) accumulate_kernel(const WeightParams p) {
   const int s = blockIdx.x / p.num_heads, h = blockIdx.x - s * p.num_heads;
-  // The lengths and rows are inputs that the decode before this kernel does
-  // not write, and it lets this one start only once what came before it is
-  // complete: they are read while it runs.
+  // The lengths, rows and tables are inputs that the decode before this kernel
+  // does not write, and it lets this one start only once what came before it
+  // is complete: they are read while it runs.
   const int n = __ldg(p.seq_lens + s);
   const int row = p.rows != nullptr ? __ldg(p.rows + s) : s;
+  const bool fine = n > 0 && n <= p.max_tokens;
+  const int entries = fine ? (n - 1) / p.block_size + 1 : 0;
+  bool bad = false;
+  for (int i = threadIdx.x; i < entries; i += kWeightThreads) {
+    const int b = __ldg(p.tables + static_cast<size_t>(s) * p.table_width + i);
+    bad |= static_cast<uint32_t>(b) >= static_cast<uint32_t>(p.num_blocks);
+  }
+  bad = __syncthreads_or(bad) != 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (n <= 0 || n > p.max_tokens) return;  // the decode has recorded a bad length
-  if (row < 0 || row >= p.num_rows) {
-    if (threadIdx.x == 0) record_status(p.status, PA_DEV_BAD_ROW);
+  if (!fine || bad) return;  // recorded by the decode
+  // The entries outlast this call: scores that a decode left unfinished are not
+  // added to them.
+  const bool failed = p.failed != nullptr && __ldcg(p.failed) != 0;
+  if (failed || row < 0 || row >= p.num_rows) {
+    if (threadIdx.x == 0) record_status(p.status, failed ? PA_DEV_TIMEOUT : PA_DEV_BAD_ROW);
     return;
   }
   float norm[G];
@@ -125,15 +139,21 @@ bool token_weights_ok(const pa_token_weights* w, int max_blocks_per_seq, int num
 }
 
 pa_status accumulate_weights(const float* scores, const float* norm2, const pa_token_weights& w,
-                             const int32_t* seq_lens, int num_seqs, int num_q_heads, int max_blocks_per_seq,
-                             int32_t* dev_status, const pa_pool_desc* pool, cudaStream_t stream) {
+                             const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                             int max_blocks_per_seq, const int32_t* failed, int32_t* dev_status,
+                             const pa_pool_desc* pool, cudaStream_t stream) {
   WeightParams p;
   p.scores = scores;
   p.norm2 = norm2;
   p.weights = w.weights;
   p.rows = w.rows;
   p.seq_lens = seq_lens;
+  p.tables = block_tables;
+  p.failed = failed;
   p.status = dev_status;
+  p.table_width = max_blocks_per_seq;
+  p.block_size = pool->block_size;
+  p.num_blocks = pool->num_blocks;
   p.max_tokens = max_blocks_per_seq * pool->block_size;
   p.score_tokens = score_tokens_of(max_blocks_per_seq, pool->block_size);
   p.row_tokens = w.row_tokens;
