@@ -509,8 +509,8 @@ typedef struct pa_token_weights {
  * max_blocks_per_seq when they pass weights (the scores of every token are
  * kept there between the two launches, 4 bytes a query head and token), else
  * 0.  It serves calls of any num_seqs and max_blocks_per_seq that it is large
- * enough for, one after another, with the same query heads, pool shape and
- * num_ctas.
+ * enough for, one after another, of either dtype, with and without weights,
+ * with the same query heads, pool shape and num_ctas.
  */
 PA_API size_t pa_decode_fp4_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
                                             int32_t weights_max_blocks_per_seq, const pa_pool_desc* pool,

@@ -485,8 +485,8 @@ static bool select_variant(const pa_pool_desc& pool, int num_q_heads, int flags,
   return false;
 }
 
-// Resident CTAs per SM times the SM count for a variant on the current
-// device; also raises the kernel's dynamic shared memory limit.  Cached per
+// CTAs per SM (the variant's own count, else the resident ones) times the SM
+// count for a variant on the current device; also raises the kernel's dynamic shared memory limit.  Cached per
 // device and kernel.
 static bool grid_size_for(const Variant& v, int& ctas) {
   struct Entry {
@@ -515,7 +515,7 @@ static bool grid_size_for(const Variant& v, int& ctas) {
     return false;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
   if (per_sm < 1) return false;
-  ctas = per_sm * sms;
+  ctas = (v.ctas_per_sm > 0 ? v.ctas_per_sm : per_sm) * sms;
   std::lock_guard<std::mutex> lock(mu);
   if (n_cache < 512) cache[n_cache++] = Entry{dev, v.kernel, ctas};
   return true;

@@ -19,6 +19,7 @@ struct Variant {
   int part_stride;  // floats per partial slot: query rows per unit * (D + 2)
   LaunchFn launch;
   int unit_cost;    // partition cost of finishing a unit (DecodeParams::unit_cost)
+  int ctas_per_sm = 0;  // of a default launch; 0: as many as the card holds of this kernel
   bool fuses_update = false;  // tensor-core decode family: takes new tokens (DecodeParams::upd_*) into its launch and writes log normalisers (DecodeParams::lse)
 };
 

@@ -850,6 +850,9 @@ ThinKernel thin_kernel(int G, Variant& v) {
   v.threads = kDecodeThreads;
   v.smem_bytes = static_cast<int>(sizeof(ThinSmem<F, kEight ? 8 : 4>));
   v.part_stride = state_floats(G, F::kD);
+  // The same count whatever registers an instance takes: the states' places, and
+  // the scores behind them, lie alike for either type and with weights or without
+  v.ctas_per_sm = F::kCtasPerSm;
   v.launch = nullptr;  // launched with its own parameters
   // what finishing a unit adds, in 1/8 granules (B200, ragged 4-bit batch: 94.3
   // us at 6, 91.4 at 10, 89.5 at 14, 91.0 at 20)
