@@ -372,6 +372,17 @@ __device__ __forceinline__ int load_acquire(const int32_t* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ int load_relaxed(const int32_t* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(int32_t* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_relaxed(int32_t* p, int v) {
+  asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 
 // Waits until every earlier chunk of the unit that reads positions [first,
 // end) has loaded its rows.  false: the limit passed.
@@ -379,7 +390,7 @@ __device__ __forceinline__ bool wait_for_readers(const int32_t* kept, int chunk,
   bool ok = true;
   for (int c = threadIdx.x; ok && c < chunk; c += kMoveThreads) {
     const int32_t* at = kept + static_cast<size_t>(c) * rows;
-    const int low = load_acquire(at), high = __ldcg(at + rows - 1);  // earlier chunks are full
+    const int low = load_acquire(at), high = load_relaxed(at + rows - 1);  // earlier chunks are full
     if (low >= 0 || position(low) >= end || position(high) < first) continue;
     const uint64_t t0 = global_timer_ns();
     while (load_acquire(at) < 0) {
@@ -480,11 +491,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   const bool wait = __syncthreads_or(in_place) != 0;  // every load of the chunk is done
-  // say so: the chunk's word is its first position, the first thread's
-  if (threadIdx.x == 0) __threadfence();
+  // Say so: the chunk's word is its first position, the first thread's.  The
+  // barrier orders the other threads' loads before its release, which a waiting
+  // CTA acquires before it stores; the other words are only looked at.
 #pragma unroll
   for (int g = 0; g < kLooks; ++g) {
-    if (token[g] >= 0) __stcg(kept + j0 + warp * kRowsWarp + lane + 32 * g, token[g]);
+    if (token[g] < 0) continue;
+    int32_t* at = kept + j0 + warp * kRowsWarp + lane + 32 * g;
+    if (g == 0 && threadIdx.x == 0) {
+      store_release(at, token[g]);
+    } else {
+      store_relaxed(at, token[g]);
+    }
   }
   if (wait && !wait_for_readers(kept, chunk, kRows, j0, j0 + kRows)) {
     if (threadIdx.x == 0) record_status(p.status, PA_DEV_TIMEOUT);
