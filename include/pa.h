@@ -574,7 +574,8 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_pool, const void
  * kept and new_lens lie apart from each other and from the integer inputs, and
  * new_weights, unless it is weights->weights, apart from that: overlaps are
  * PA_ERR_INVALID_ARG.  max_blocks_per_seq * block_size is at most 2^30.
- *   fp4          1: the pools are 4-bit pools, else 0
+ *   fp4          1: the pools are 4-bit pools, else 0 (a test adds
+ *                PA_EVICT_TEST_WITHHOLD)
  * Blocks of 8, 16 or 32 tokens and head_dim 64 or 128.  Device errors:
  * PA_DEV_BAD_SEQ_LEN (treated as empty: new_lens 0), PA_DEV_BAD_ROW and
  * PA_DEV_BAD_BUDGET (m > max_kept), which leave the sequence as it is, and
@@ -582,6 +583,12 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_pool, const void
  * PA_DEV_TIMEOUT (a wait of 2 s for other blocks of the launch ran out: the
  * call's pools and weights are then unusable).
  */
+/* Failure-detection test hook, added to pa_evict's fp4: the first rows of
+ * sequence 0's kv head 0 are loaded, but nobody is told, and they are not
+ * stored; waits for them run out after about 20 ms, and the call ends with
+ * PA_DEV_TIMEOUT.  Never set it outside such tests. */
+#define PA_EVICT_TEST_WITHHOLD 256
+
 PA_API pa_status pa_evict(const int32_t* block_tables, const int32_t* dst_tables, int32_t max_blocks_per_seq,
                           const int32_t* seq_lens, int32_t num_seqs, const int32_t* budgets, int32_t sinks,
                           int32_t recent, const pa_token_weights* weights, float* new_weights, int32_t* kept,

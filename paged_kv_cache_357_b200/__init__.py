@@ -36,6 +36,7 @@ from ._lib import (  # noqa: F401
     PA_DECODE_CUDA_CORES_ONLY,
     PA_DECODE_TEST_SKIP_UPDATE_ARRIVAL,
     PA_DECODE_TEST_WITHHOLD_COPIES,
+    PA_EVICT_TEST_WITHHOLD,
     PA_FP16,
     CacheUpdate,
     DecodeOpts,

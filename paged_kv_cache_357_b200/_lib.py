@@ -20,6 +20,7 @@ PA_FP16, PA_BF16 = 0, 1
 PA_DECODE_TEST_WITHHOLD_COPIES = 1
 PA_DECODE_CUDA_CORES_ONLY = 2
 PA_DECODE_TEST_SKIP_UPDATE_ARRIVAL = 4
+PA_EVICT_TEST_WITHHOLD = 256
 DEV_STATUS = {
     0: "PA_DEV_OK",
     101: "PA_DEV_BAD_BLOCK_ID",

@@ -379,13 +379,14 @@ def _want_evict(block_tables, seq_lens, budgets, kept, new_lens, k_pool, v_pool,
 
 def pa_evict(block_tables, seq_lens, budgets, weights, kept, new_lens, k_pool, v_pool, sinks: int = 0,
              recent: int = 0, dst_tables=None, new_weights=None, weight_rows=None, dev_status=None,
-             stream=None) -> None:
+             stream=None, flags: int = 0) -> None:
     """Keep budgets[s] tokens of each sequence (negative: leave it) by their
     accumulated weights, beside its first `sinks` and last `recent` ones, and
     move them together in their order (pa_evict).  Pools are 16-bit, or uint8
     for 4-bit ones.  kept [num_seqs, num_kv_heads, room] int32 and new_lens
     [num_seqs] int32 are written; dst_tables and new_weights are where the
-    rows and weights go, in place when None."""
+    rows and weights go, in place when None.  flags: 0, or the test hook
+    PA_EVICT_TEST_WITHHOLD."""
     index, (nb, hkv, bs, row), S, width, room = _want_evict(block_tables, seq_lens, budgets, kept, new_lens, k_pool,
                                                             v_pool, dst_tables)
     fp4 = k_pool.dtype is torch.uint8
@@ -397,5 +398,5 @@ def pa_evict(block_tables, seq_lens, budgets, weights, kept, new_lens, k_pool, v
             raise ValueError("new_weights must have weights' shape")
     _run("pa_evict", index, _lib.pa_evict, block_tables.data_ptr(), _ptr(dst_tables), width, seq_lens.data_ptr(), S,
          budgets.data_ptr(), sinks, recent, ctypes.byref(tw), _ptr(new_weights), kept.data_ptr(), room,
-         new_lens.data_ptr(), int(fp4), k_pool.data_ptr(), v_pool.data_ptr(), _status_ptr(dev_status, index), desc,
+         new_lens.data_ptr(), fp4 | flags, k_pool.data_ptr(), v_pool.data_ptr(), _status_ptr(dev_status, index), desc,
          _stream_of(index, stream))

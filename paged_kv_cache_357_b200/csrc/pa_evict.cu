@@ -63,7 +63,6 @@ constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kRounds = 8;      // 512-byte copies a warp has in flight
 constexpr int kChunkBytes = kMoveWarps * kRounds * 512;
 constexpr int kMaxCluster = 8;  // the largest portable one
-constexpr unsigned long long kWaitNs = 2ull * 1000 * 1000 * 1000;
 
 struct EvictParams {
   const int32_t* tables;
@@ -84,6 +83,8 @@ struct EvictParams {
   int sinks, recent;
   int log2_block;
   int tile;                  // bytes of a (block, kv head)
+  int withhold;              // PA_EVICT_TEST_WITHHOLD
+  unsigned long long wait_limit_ns;
 };
 
 // What happens to sequence s: its tokens, how many stay, its row of weights;
@@ -386,7 +387,8 @@ __device__ __forceinline__ void store_relaxed(int32_t* p, int v) {
 
 // Waits until every earlier chunk of the unit that reads positions [first,
 // end) has loaded its rows.  false: the limit passed.
-__device__ __forceinline__ bool wait_for_readers(const int32_t* kept, int chunk, int rows, int first, int end) {
+__device__ __forceinline__ bool wait_for_readers(const int32_t* kept, int chunk, int rows, int first, int end,
+                                                 unsigned long long limit_ns) {
   bool ok = true;
   for (int c = threadIdx.x; ok && c < chunk; c += kMoveThreads) {
     const int32_t* at = kept + static_cast<size_t>(c) * rows;
@@ -394,7 +396,7 @@ __device__ __forceinline__ bool wait_for_readers(const int32_t* kept, int chunk,
     if (low >= 0 || position(low) >= end || position(high) < first) continue;
     const uint64_t t0 = global_timer_ns();
     while (load_acquire(at) < 0) {
-      if (global_timer_ns() - t0 > kWaitNs) {
+      if (global_timer_ns() - t0 > limit_ns) {
         ok = false;
         break;
       }
@@ -491,6 +493,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   const bool wait = __syncthreads_or(in_place) != 0;  // every load of the chunk is done
+  if (p.withhold && blockIdx.x == 0) return;
   // Say so: the chunk's word is its first position, the first thread's.  The
   // barrier orders the other threads' loads before its release, which a waiting
   // CTA acquires before it stores; the other words are only looked at.
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
       store_relaxed(at, token[g]);
     }
   }
-  if (wait && !wait_for_readers(kept, chunk, kRows, j0, j0 + kRows)) {
+  if (wait && !wait_for_readers(kept, chunk, kRows, j0, j0 + kRows, p.wait_limit_ns)) {
     if (threadIdx.x == 0) record_status(p.status, PA_DEV_TIMEOUT);
     return;
   }
@@ -586,13 +589,14 @@ using namespace pa::evict;
 extern "C" pa_status pa_evict(const int32_t* block_tables, const int32_t* dst_tables, int32_t max_blocks_per_seq,
                               const int32_t* seq_lens, int32_t num_seqs, const int32_t* budgets, int32_t sinks,
                               int32_t recent, const pa_token_weights* weights, float* new_weights, int32_t* kept,
-                              int32_t max_kept, int32_t* new_lens, int32_t fp4_pools, void* k_pool, void* v_pool,
+                              int32_t max_kept, int32_t* new_lens, int32_t fp4, void* k_pool, void* v_pool,
                               int32_t* dev_status, const pa_pool_desc* pool, void* stream) {
   if (pool == nullptr || pool->num_blocks <= 0 || pool->num_kv_heads <= 0 || num_seqs < 0 || max_blocks_per_seq <= 0 ||
-      sinks < 0 || recent < 0 || max_kept < 0 || (fp4_pools != 0 && fp4_pools != 1))
+      sinks < 0 || recent < 0 || max_kept < 0 || (fp4 & ~(1 | PA_EVICT_TEST_WITHHOLD)) != 0)
     return PA_ERR_INVALID_ARG;
-  if (!fp4::pool_ok(pool)) return PA_ERR_UNSUPPORTED;  // the same block sizes and head_dims in both kinds of pool
-  if (static_cast<long long>(max_blocks_per_seq) * pool->block_size > fp4::kMaxTokens) return PA_ERR_INVALID_ARG;
+  const bool fp4_pools = (fp4 & 1) != 0, withhold = (fp4 & PA_EVICT_TEST_WITHHOLD) != 0;
+  if (!pa::fp4::pool_ok(pool)) return PA_ERR_UNSUPPORTED;  // the same block sizes and head_dims in both kinds of pool
+  if (static_cast<long long>(max_blocks_per_seq) * pool->block_size > pa::fp4::kMaxTokens) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
   auto aligned4 = [](const void* x) { return x != nullptr && (reinterpret_cast<uintptr_t>(x) & 3u) == 0; };
   if (!aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(budgets) || !aligned4(new_lens) ||
@@ -639,8 +643,10 @@ extern "C" pa_status pa_evict(const int32_t* block_tables, const int32_t* dst_ta
   p.max_tokens = max_blocks_per_seq * pool->block_size;
   p.sinks = sinks;
   p.recent = recent;
-  p.log2_block = fp4::log2_of(pool->block_size);
-  p.tile = fp4_pools ? fp4::tile_bytes(pool->block_size, pool->head_dim) : pool->block_size * pool->head_dim * 2;
+  p.log2_block = pa::fp4::log2_of(pool->block_size);
+  p.tile = fp4_pools ? pa::fp4::tile_bytes(pool->block_size, pool->head_dim) : pool->block_size * pool->head_dim * 2;
+  p.withhold = withhold;
+  p.wait_limit_ns = withhold ? 20ull * 1000 * 1000 : 2ull * 1000 * 1000 * 1000;
   const long long units = static_cast<long long>(num_seqs) * pool->num_kv_heads;
   const long long rows = max_kept < p.max_tokens ? max_kept : p.max_tokens;  // at most, of a sequence
   if (units * kMaxCluster > 0x7fffffffLL) return PA_ERR_INVALID_ARG;
