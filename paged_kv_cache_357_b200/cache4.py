@@ -30,13 +30,14 @@ _lib = None
 
 def _bind() -> None:
     global torch, _raw_stream, _current_device, _lib
-    torch = _torch()
-    _codes.update({torch.float16: PA_FP16, torch.bfloat16: PA_BF16})
+    t = _torch()
     _lib = load()
+    _codes.update({t.float16: PA_FP16, t.bfloat16: PA_BF16})
     # the handle without a Stream object around it, where this torch has it
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: t.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    torch = t  # last: a thread that sees it finds the rest bound
 
 
 def _want(t, name, dtype, ndim, index) -> None:
