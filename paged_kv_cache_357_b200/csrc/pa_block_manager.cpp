@@ -268,34 +268,57 @@ extern "C" pa_status pa_bm_prepare_eviction(pa_block_manager* bm, const int64_t*
     dropped += static_cast<int64_t>(seqs[i]->blocks.size()) - keep;
   }
   if (fresh > static_cast<int64_t>(bm->free_list.size())) return PA_ERR_OUT_OF_BLOCKS;
+  struct Move {
+    int32_t i, j;  // block j of sequence i gives way to a fresh one
+  };
+  std::vector<Move> moves;
   std::vector<int32_t> give_back;
+  moves.reserve(static_cast<size_t>(fresh));
   give_back.reserve(static_cast<size_t>(fresh + dropped));
   auto fill = [&](int32_t* row, const std::vector<int32_t>& blocks) {
     std::copy(blocks.begin(), blocks.end(), row);
     std::fill(row + blocks.size(), row + max_blocks_per_seq, -1);
   };
   for (int32_t i = 0; i < n; ++i) {
-    fill(block_tables + static_cast<size_t>(i) * max_blocks_per_seq, seqs[i]->blocks);
-    seq_lens[i] = seqs[i]->tokens;
+    const auto& s = *seqs[i];
+    fill(block_tables + static_cast<size_t>(i) * max_blocks_per_seq, s.blocks);
+    seq_lens[i] = s.tokens;
+    if (!cut(i)) continue;
+    const int32_t keep = bm->blocks_for(budgets[i]);
+    for (int32_t j = 0; j < keep; ++j) {
+      if (bm->ref[s.blocks[j]] > 1) {
+        moves.push_back(Move{i, j});
+        give_back.push_back(s.blocks[j]);
+      }
+    }
+    give_back.insert(give_back.end(), s.blocks.begin() + keep, s.blocks.end());
   }
-  // nothing below allocates but the free set, when blocks return to it
+  // The references first: blocks at zero join the free set behind those that
+  // the fresh ones are taken from.  Its growth is the last allocation, and is
+  // taken back if it fails.
+  size_t done = 0, freed = 0;
+  try {
+    for (; done < give_back.size(); ++done) {
+      const int32_t b = give_back[done];
+      if (bm->ref[b] == 1) {
+        bm->free_list.push_back(b);
+        ++freed;
+      }
+      bm->ref[b] -= 1;
+    }
+  } catch (...) {
+    while (done > 0) bm->ref[give_back[--done]] += 1;
+    for (; freed > 0; --freed) bm->free_list.pop_back();
+    throw;
+  }
+  for (const Move& m : moves) seqs[m.i]->blocks[m.j] = bm->take();
   for (int32_t i = 0; i < n; ++i) {
     if (cut(i)) {
-      auto& s = *seqs[i];
-      const int32_t keep = bm->blocks_for(budgets[i]);
-      for (int32_t j = 0; j < keep; ++j) {
-        if (bm->ref[s.blocks[j]] > 1) {
-          give_back.push_back(s.blocks[j]);
-          s.blocks[j] = bm->take();
-        }
-      }
-      for (size_t j = keep; j < s.blocks.size(); ++j) give_back.push_back(s.blocks[j]);
-      s.blocks.resize(keep);
-      s.tokens = budgets[i];
+      seqs[i]->blocks.resize(bm->blocks_for(budgets[i]));
+      seqs[i]->tokens = budgets[i];
     }
     fill(dst_tables + static_cast<size_t>(i) * max_blocks_per_seq, seqs[i]->blocks);
   }
-  for (int32_t b : give_back) bm->release(b);
   return PA_OK;
 } catch (...) {  // out of host memory
   return PA_ERR_INVALID_ARG;
