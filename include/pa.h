@@ -571,8 +571,8 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_pool, const void
  *   kept         int32 device [num_seqs][num_kv_heads][max_kept]; entries
  *                past m are left as they were
  *   new_lens     int32 device [num_seqs]
- * kept and new_lens lie apart from each other and from the integer inputs, and
- * new_weights, unless it is weights->weights, apart from that: overlaps are
+ * kept, new_lens and (unless it is weights->weights) new_weights lie apart from
+ * each other, from the integer inputs and from the weights: overlaps are
  * PA_ERR_INVALID_ARG.  max_blocks_per_seq * block_size is at most 2^30.
  *   fp4          1: the pools are 4-bit pools, else 0 (a test adds
  *                PA_EVICT_TEST_WITHHOLD)

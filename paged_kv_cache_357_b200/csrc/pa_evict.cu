@@ -608,17 +608,18 @@ extern "C" pa_status pa_evict(const int32_t* block_tables, const int32_t* dst_ta
   const size_t seqs = static_cast<size_t>(num_seqs), heads = static_cast<size_t>(pool->num_kv_heads);
   {  // what is written while the inputs may still be read
     const size_t table = seqs * max_blocks_per_seq * 4;
+    const Span all{weights->weights,
+                   static_cast<size_t>(weights->num_rows) * heads * static_cast<size_t>(weights->row_tokens) * 4};
     const Span in[] = {{seq_lens, seqs * 4}, {budgets, seqs * 4}, {weights->rows, seqs * 4}, {block_tables, table},
-                       {dst_tables, table}};
-    const Span out[] = {{new_lens, seqs * 4}, {kept, seqs * heads * max_kept * 4}};
+                       {dst_tables, table}, all};
+    const Span moved{new_weights != weights->weights ? new_weights : nullptr, all.bytes};
+    const Span out[] = {{new_lens, seqs * 4}, {kept, seqs * heads * max_kept * 4}, moved};
     for (const Span& o : out) {
       for (const Span& i : in) {
         if (overlap(o, i)) return PA_ERR_INVALID_ARG;
       }
     }
-    if (overlap(out[0], out[1])) return PA_ERR_INVALID_ARG;
-    const size_t all = static_cast<size_t>(weights->num_rows) * heads * static_cast<size_t>(weights->row_tokens) * 4;
-    if (new_weights != weights->weights && overlap({new_weights, all}, {weights->weights, all})) return PA_ERR_INVALID_ARG;
+    if (overlap(out[0], out[1]) || overlap(out[0], moved) || overlap(out[1], moved)) return PA_ERR_INVALID_ARG;
   }
   EvictParams p;
   p.tables = block_tables;
