@@ -135,6 +135,14 @@ def _status_ptr(dev_status, index):
     return dev_status.data_ptr()
 
 
+def _int32(x, name) -> int:
+    """x, which a C int holds (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return x
+
+
 def _token_weights(weights, weight_rows, num_new, num_seqs, num_kv_heads, tokens, index) -> TokenWeights:
     """The pa_token_weights of weights [rows, num_kv_heads, row_tokens]."""
     _want(weights, "weights", torch.float32, 3, index)
@@ -147,7 +155,7 @@ def _token_weights(weights, weight_rows, num_new, num_seqs, num_kv_heads, tokens
             raise ValueError("weight_rows must have num_seqs entries")
     elif rows < num_seqs:
         raise ValueError("weights must have a row for every sequence")
-    return TokenWeights(weights.data_ptr(), row_tokens, _ptr(weight_rows), rows, int(num_new))
+    return TokenWeights(weights.data_ptr(), row_tokens, _ptr(weight_rows), rows, _int32(num_new, "num_new"))
 
 
 # ---------------------------------------------------------------------------
@@ -398,6 +406,6 @@ def pa_evict(block_tables, seq_lens, budgets, weights, kept, new_lens, k_pool, v
         if new_weights.shape != weights.shape:
             raise ValueError("new_weights must have weights' shape")
     _run("pa_evict", index, _lib.pa_evict, block_tables.data_ptr(), _ptr(dst_tables), width, seq_lens.data_ptr(), S,
-         budgets.data_ptr(), sinks, recent, ctypes.byref(tw), _ptr(new_weights), kept.data_ptr(), room,
+         budgets.data_ptr(), _int32(sinks, "sinks"), _int32(recent, "recent"), ctypes.byref(tw), _ptr(new_weights), kept.data_ptr(), room,
          new_lens.data_ptr(), fp4 | flags, k_pool.data_ptr(), v_pool.data_ptr(), _status_ptr(dev_status, index), desc,
          _stream_of(index, stream))
