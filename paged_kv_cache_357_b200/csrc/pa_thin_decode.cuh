@@ -529,9 +529,10 @@ __device__ __forceinline__ int arrive(int32_t* count, int n) {
 // The merge of the states of a unit's pieces, piece(0), piece(1), ...: the
 // online-softmax rule with the largest m as the common reference.  More than
 // 2 kFan pieces are merged in two levels, kFan neighbours by the last of them
-// to arrive and the groups by the last group: a call of 8 units of 38k tokens
-// over 592 CTAs takes 22 us, and 42 where one CTA merges a unit's 74 pieces;
-// one of a sequence in 10 to 16 pieces 10.4 us in one level and 11.7 in two.
+// to arrive and the groups by the last group.  Over the 444 CTAs of a default
+// launch, two sequences of 38k tokens, G = 4 to 8: 8 units of 55 pieces 23.7 us
+// in two levels and 28.6 where one CTA merges them all, 16 units of 28 pieces
+// 28.4 and 28.7, 26 units of 17 pieces 38.7 and 38.0.
 //
 // A few pieces, by one warp: a lane's elements 4 (lane + 32 j), two j at a
 // time with all their loads on the way together.
