@@ -36,10 +36,10 @@
 // Measured (B200, 8 kv heads, D = 128, 16-bit pools): 64 sequences of 1040
 // tokens cut to 1024 in place 96 us, 5.6 TB/s (0.86 of the copy rate); 16 of
 // about 5000 cut to 1024 into fresh blocks 37 us, 3.5 TB/s; two of 65536 cut to
-// 16384 in place 83 us, 3.3 TB/s.  The last two pay for the selection first
-// (about 11 and 22 us of dependent passes over a cluster's histograms; 1 and 4
-// more when all three were always made), then for rows of 256 bytes that lie
-// apart.  Clusters that moved 64 KB batches behind barriers took 128, 50 and
+// 16384 in place 84 us, 3.3 TB/s (4-bit pools: 40, 30 and 51 us).  The last two
+// pay for the selection first (about 11 and 22 us of dependent passes over a
+// cluster's histograms; 1 and 4 more when all three were always made), then for
+// rows of 256 bytes that lie apart.  Clusters that moved 64 KB batches behind barriers took 128, 50 and
 // 130 us; a persistent, pipelined form of them 148 where they took 106.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

@@ -9,11 +9,15 @@
 // and neighbouring threads touch neighbouring bytes; the two threads of a
 // group exchange their maxima.  Each thread has kUnroll such pieces on the way.
 //
-// Measured (B200, D = 128, 8 kv heads, bf16): a store of 16384 tokens and a
-// read-back of them take 34.8 us together for 172 MB, 4.9 TB/s (0.75 of the copy
-// rate); 44 with 8 bytes a thread and load, 37 with divisions instead of a
-// reciprocal rounded to where midpoints are exact.  The scales' single-byte
-// stores and the slots' lookups are what is left.  256 tokens: 4.4 us for both.
+// Measured (B200, D = 128, 8 kv heads, bf16; in a captured graph): a store of
+// 16384 tokens 19.8 us, 4.4 TB/s (0.66 of the copy rate), whether their slots
+// are scattered or whole blocks in order; their read-back 17.3 us, 5.0 TB/s
+// (0.76); the two in turn 35.7, and 35.9 through the Python entry points.  What
+// bounds them is instructions: 0.73 and 0.79 issued a cycle, DRAM a third busy.
+// 44 us with 8 bytes a thread and load, 37 with divisions instead of a
+// reciprocal rounded to where midpoints are exact.  A decode step's 256 tokens:
+// 2.4 us on the GPU, 5.9 through the entry point.  Block copies: 4096 pairs 24.8
+// us, 6.1 TB/s (0.93), 96 pairs 2.2.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -14,7 +14,11 @@
 // memories that carry 128 bytes a cycle, twice (write and operand read); so
 // the codes go from shared memory into registers, are expanded there and
 // enter mma.sync as the A operand straight from those registers.  The thin
-// products (at most 8 query rows) need a third of that path's rate.
+// products (at most 8 query rows) need a third of that path's rate.  Not tried:
+// K alone as the packed operand of a block-scaled tcgen05.mma, which takes e2m1
+// with an e4m3 scale per 16 elements along the contraction as they lie here, and
+// q as several e2m1 digits.  V's scales run along the output's rows, so V would
+// be expanded as now.
 //
 // Rows (the kernel: pa_thin_decode.cuh).  p enters as a half and the half of its
 // rounding residual.  A half alone, off by up to 2^-11 of each weight, would do
@@ -33,17 +37,17 @@
 // operations for 16 codes) before they are expanded.  p^T is transposed by
 // movmatrix.
 //
-// Measured (B200, one launch, D = 128): 8 sequences of 32k tokens x 40 kv heads,
-// G = 1, fp16: 274 us, 5.5 TB/s (0.84 of the copy rate; under the power cap of
-// a long loop 327); 256 sequences of log-normal lengths (median 1024) x 8, G =
-// 4, bf16: 93 us, 4.2 TB/s; one sequence of 1027 tokens x 8, G = 4: 10.  What
-// is left of the roof goes to instructions: about 310 for 16 tokens and a kv
-// head, issued at 0.57 a clock, with the pipe of the conversions half busy and
-// the tensor pipe a quarter.  The warps do not wait for memory: 3 CTAs an SM
-// (168 registers, no spills) take 274 us where 2 take 298, 4 take 280 and 5 (96
-// registers) twice as much; copies by TMA instead of cp.async and ranges
-// weighted by the CTAs' age measured slower (294 and 334 us where 4 CTAs took
-// 280 and 290).
+// Measured (B200, one launch, D = 128, in a captured graph): 8 sequences of 32k
+// tokens x 40 kv heads, G = 1, fp16: 275 us, 5.5 TB/s (0.84 of the copy rate;
+// under the power cap of a long loop through the entry point 323); 256 sequences
+// of log-normal lengths (median 1024) x 8, G = 4, bf16: 93 us, 4.2 TB/s, 99
+// through the entry point; one sequence of 1027 tokens x 8, G = 4: 10.  What is
+// left of the roof goes to instructions: about 320 for 16 tokens and a kv head,
+// issued at 0.58 a clock, with the pipe of the conversions half busy and the
+// tensor pipe a quarter.  The warps do not wait for memory: 3 CTAs an SM (168
+// registers, no spills) took 274 us where 2 took 298, 4 took 280 and 5 (96
+// registers) twice as much; copies by TMA instead of cp.async and ranges weighted
+// by the CTAs' age measured slower (294 and 334 us where 4 CTAs took 280 and 290).
 #include <cuda_runtime.h>
 
 #include <cmath>

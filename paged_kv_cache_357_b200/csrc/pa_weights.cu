@@ -15,11 +15,12 @@
 // once read) and 8 of weights a (token, kv head), one thread each, in the
 // order of memory.
 //
-// Measured (B200): decode and weights of 256 sequences (log-normal lengths,
-// median 1024, 8 kv heads, G = 4, D = 128, 16-bit pools) 237 us, 5.9 TB/s of
-// what the two must move (0.91 of the copy rate); 245 with scores that go to
-// memory and come back.  128 sequences of 2304 tokens, G = 8, 4-bit pools: 113
-// us, of which this launch is about 12.
+// Measured (B200, in a captured graph): decode and weights of 256 sequences
+// (log-normal lengths, median 1024, 8 kv heads, G = 4, D = 128, 16-bit pools) 237
+// us, 5.9 TB/s of what the two must move (0.90 of the copy rate), 245 through the
+// entry point; 8 more with scores that go to memory and come back.  128 sequences
+// of 2304 tokens, G = 8, 4-bit pools: 113 us (120), of which this launch is about
+// 12.  The look at the table's entries (see accumulate_kernel) is 2 us of each.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -14,9 +14,9 @@
 // conflict.
 //
 // Bound by memory.  Measured (B200, decode and weights, both launches): 64
-// sequences of 2000 tokens x 8 kv heads, G = 4, bf16: 53.3 us, 4.9 TB/s (0.75
+// sequences of 2000 tokens x 8 kv heads, G = 4, bf16: 56 us, 4.7 TB/s (0.71
 // of the copy rate), 131 on CUDA cores; 5 sequences of at most 100 tokens x 4:
-// 7.9 us, 14.5 on CUDA cores.
+// 7.7 us, 14.5 on CUDA cores.
 #include <cuda_runtime.h>
 
 #include <cstdint>
