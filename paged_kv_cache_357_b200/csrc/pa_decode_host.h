@@ -19,8 +19,8 @@ struct Variant {
   int part_stride;  // floats per partial slot: query rows per unit * (D + 2)
   LaunchFn launch;
   int unit_cost;    // partition cost of finishing a unit (DecodeParams::unit_cost)
-  int ctas_per_sm = 0;  // of a default launch; 0: as many as the card holds of this kernel
   bool fuses_update = false;  // tensor-core decode family: takes new tokens (DecodeParams::upd_*) into its launch and writes log normalisers (DecodeParams::lse)
+  int ctas_per_sm = 0;  // of a default launch; 0: as many as the card holds of this kernel
 };
 
 // Tensor-core variants (pa_attn_tc.cuh), if one exists for this pool and
