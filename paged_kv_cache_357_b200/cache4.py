@@ -17,8 +17,8 @@ import ctypes
 from functools import lru_cache
 from typing import Tuple
 
-from ._lib import (PA_BF16, PA_FP16, DecodeOpts, PaError, PoolDesc, TokenWeights, _dtype_code, _need, _ptr, _torch,
-                   load, pool_desc)
+from ._lib import (PA_BF16, PA_EVICT_TEST_WITHHOLD, PA_FP16, DecodeOpts, PaError, PoolDesc, TokenWeights, _dtype_code,
+                   _need, _ptr, _torch, load, pool_desc)
 
 # bound at the first call, with torch and the library loaded (_bind)
 torch = None
@@ -405,7 +405,9 @@ def pa_evict(block_tables, seq_lens, budgets, weights, kept, new_lens, k_pool, v
         _want(new_weights, "new_weights", torch.float32, 3, index)
         if new_weights.shape != weights.shape:
             raise ValueError("new_weights must have weights' shape")
+    if flags != 0 and flags != PA_EVICT_TEST_WITHHOLD:  # the bits below are not the caller's
+        raise PaError(1, "pa_evict")
     _run("pa_evict", index, _lib.pa_evict, block_tables.data_ptr(), _ptr(dst_tables), width, seq_lens.data_ptr(), S,
-         budgets.data_ptr(), _int32(sinks, "sinks"), _int32(recent, "recent"), ctypes.byref(tw), _ptr(new_weights), kept.data_ptr(), room,
-         new_lens.data_ptr(), fp4 | flags, k_pool.data_ptr(), v_pool.data_ptr(), _status_ptr(dev_status, index), desc,
-         _stream_of(index, stream))
+         budgets.data_ptr(), _int32(sinks, "sinks"), _int32(recent, "recent"), ctypes.byref(tw), _ptr(new_weights),
+         kept.data_ptr(), room, new_lens.data_ptr(), fp4 | flags, k_pool.data_ptr(), v_pool.data_ptr(),
+         _status_ptr(dev_status, index), desc, _stream_of(index, stream))
